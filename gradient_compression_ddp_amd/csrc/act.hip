@@ -50,12 +50,15 @@ __device__ __forceinline__ float gelu_tail(float z, float e) {   // Q(z), e = ex
 
 constexpr float kLog2e = 1.44269504f;
 
-// 1 / (1 + exp(-u)).  The hardware's exp2 and reciprocal flush results below 2^-126, where
-// f' still multiplies p by some hundreds: they work on 2^-64 (1 + exp(-u)) instead, and the
-// last product, which does not flush, scales back.
+// 1 / (1 + exp(-u)).  The hardware's exp2 and reciprocal flush results below 2^-126, where f' still multiplies p by some
+// hundreds: far out they work on 2^-64 (1 + exp(-u)) instead, and the last product, which does not flush, scales back.
+// Only there: the shift rounds the exponent at its own size of 64, 2e-6 of p, where u itself is small (p was
+// off by up to 1.4e-6 for |u| < 1 with the shift everywhere, and is by 1.2e-7 now).  Past -40 the shifted
+// exponent is the smaller one.
 __device__ __forceinline__ float sigmoid(float u) {
-  constexpr float k = 5.42101086e-20f;                       // 2^-64
-  return k * rcp_hw(k + exp2_hw(__builtin_fmaf(u, -kLog2e, -64.0f)));
+  const bool far = u < -40.0f;
+  const float k = far ? 5.42101086e-20f : 1.0f;              // 2^-64
+  return k * rcp_hw(k + exp2_hw(__builtin_fmaf(u, -kLog2e, far ? -64.0f : 0.0f)));
 }
 
 template <int KIND>

@@ -1,0 +1,50 @@
+"""The training-step operators where their arithmetic, their row walks and their arguments have edges, against the
+float64 oracle.  u = 2^-24 is fp32's rounding; the hardware's exp2 and reciprocal are off by 2 u each."""
+import numpy as np
+import pytest
+
+from oracle import train as o
+from test_gpu_train import U, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gc():
+    import gradient_compression_ddp_amd as lib
+    return lib
+
+
+# --- the activations' own roundings ---------------------------------------------------------
+
+def p_bound(p, arg, arg_rel):
+    """Relative error of p = 1 / (1 + exp(-arg)) in units of u, arg itself off by arg_rel u: the exponent's
+    rounding and its constant (1.25 u of arg), exp2 (2), of which p sees the share 1 - p; sum (1), reciprocal (2)."""
+    return (1 - p) * (2 + (1.25 + arg_rel) * np.abs(arg)) + 3
+
+
+@pytest.mark.parametrize("kind,arg_rel", [("silu", 0), ("gelu_tanh", 6)])
+@pytest.mark.parametrize("top", [1, 6, 100])
+def test_sigmoid_kinds_are_as_exact_as_fp32(gc, kind, arg_rel, top):
+    """gelu_tanh's argument: two constants' product (3), the square (1), the sum and the last product (1 each)."""
+    import torch
+    x = torch.from_numpy(np.linspace(-top, top, 40003)).float().cuda()[None]
+    dy = torch.full_like(x, 0.75)
+    v, d = host(x), 0.75
+    p, s = o.act_parts(v, kind)
+    c = np.clip(v, -32, 32)
+    arg = v if kind == "silu" else 2 * np.sqrt(2 / np.pi) * (c + 0.044715 * c ** 3)
+    e = p_bound(p, arg, arg_rel)
+    off = np.abs(host(gc.act_forward(x, kind)[0]) - v * p)
+    # 2^-149: the least fp32 number, which p and the result are rounded to at their smallest
+    assert (off <= 1.01 * U * (e + 1) * np.abs(v * p) + (1 + np.abs(v)) * 2.0 ** -149).all(), (off / (U * np.abs(v * p) + 1e-300)).max()
+    # 1 - p is off by p's error and its own rounding
+    rest = e * p + (1 - p)
+    if kind == "silu":           # p (1 + x (1 - p))
+        b = e * np.abs(p + s) + p * (np.abs(v) * rest + np.abs(1 + v * (1 - p))) + np.abs(p + s)
+    else:                        # p + (c u') (p (1 - p)), c u' off by 7 u
+        cdu = c * 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * c * c)
+        b = e * p + np.abs(s) * (8 + e) + np.abs(cdu) * p * rest + np.abs(p + s)
+    got = host(gc.act_backward(dy, kind, x=x))
+    off = np.abs(got - d * (p + s))
+    assert (off <= 1.01 * U * d * (b + np.abs(p + s)) + (1 + np.abs(v)) ** 3 * 2.0 ** -148).all()
