@@ -19,13 +19,16 @@ constexpr int kThreads = 256;
 constexpr int kNone = -1;
 
 // ---------------------------------------------------------------------------------
-// The activations.  Both tails keep their relative precision.
+// The activations, in fp32.  No tail is a difference of larger numbers, so each keeps its relative precision but for the
+// rounding of its exponent, which grows with the exponent's size.
 //
 // GELU.  With z = |x| and Q(z) = 1 - Phi(z) = exp(-z^2/2) * R(t), t = 1 / (1 + 0.23 z): R is
 // the scaled complementary error function, smooth in t, fitted here by a polynomial of degree
-// 8 with a relative error of 4.8e-8 for z in [0, 14.5] (beyond that exp(-z^2/2) is below
-// 2^-149); in fp32 the whole is good to 5e-7 relative.  Phi(x) is Q(z) for x < 0 and 1 - Q(z) otherwise, and
-// f'(x) = Phi(x) + x * exp(-x^2/2) / sqrt(2 pi) takes the same exponential.
+// 8 with a relative error of 4.8e-8 for z in [0, 14.5].  Phi(x) is Q(z) for x < 0 and 1 - Q(z) otherwise, and
+// f'(x) = Phi(x) + x * exp(-x^2/2) / sqrt(2 pi) takes the same exponential.  Q is good to 5e-7 relative up to z = 2; beyond,
+// the exponent z^2/2 is rounded twice at its own size, 2^-24 of it each: 2e-6 at z = 5, 8e-6 at z = 11.  That is what
+// rounding z itself once costs, and results of 16 bits do not see it.  Past z = 13.2 the hardware's exp2 gives 0:
+// x Q(z) and f', which are below 2^-122 there, are 0.
 //
 // The tanh form is x * p with p = 1 / (1 + exp(-u)), u = 2 sqrt(2/pi) (x + 0.044715 x^3), and
 // f' = p + x p (1 - p) u'.  Past |x| = 32, p is 0 or 1 and p (1 - p) is 0 in fp32, so x is limited there before

@@ -48,3 +48,21 @@ def test_sigmoid_kinds_are_as_exact_as_fp32(gc, kind, arg_rel, top):
     got = host(gc.act_backward(dy, kind, x=x))
     off = np.abs(got - d * (p + s))
     assert (off <= 1.01 * U * d * (b + np.abs(p + s)) + (1 + np.abs(v)) ** 3 * 2.0 ** -148).all()
+
+
+def test_gelu_tail_is_as_exact_as_stated(gc):
+    """x Phi(x) for x < 0, in units of u: the exponent z^2/2 (its square, its constant and their product: 2.25 of it), exp2
+    (2); t = 1 / (1 + 0.23 z) (4, and R goes at most as t); R's eight steps and constants (6), its fit (1), the two
+    last products (2).  Past z = 13.2, where exp(-z^2/2) < 2^-126, 0 is allowed."""
+    import torch
+    x = torch.from_numpy(np.linspace(-16, 0, 40003)).float().cuda()[None]
+    v = host(x)
+    want = o.act_forward(v, "gelu")
+    off = np.abs(host(gc.act_forward(x, "gelu")[0]) - want)
+    bound = 1.01 * U * (15 + 2.25 * v * v / 2) * np.abs(want)
+    assert (off <= np.where(v < -13.2, np.abs(want), bound)).all(), (off / (U * np.abs(want) + 1e-300)).max()
+    p, s = o.act_parts(v, "gelu")
+    # f' = Q - z phi: each by its own bound (phi: the exponent's, its constant and two roundings)
+    off = np.abs(host(gc.act_backward(torch.ones_like(x), "gelu", x=x)) - (p + s))
+    bound = 1.01 * U * ((15 + 2.25 * v * v / 2) * p + (6 + 2.25 * v * v / 2) * np.abs(s) + np.abs(p + s))
+    assert (off <= np.where(v < -13.2, np.abs(p + s), bound)).all()
