@@ -49,11 +49,13 @@ class _MlpBlock(torch.autograd.Function):
 
 
 def mlp_block8(x, ln_w, ln_b, w1, b1, w2, b2, kind="gelu", eps=1e-5):
-    """The block as a function; x [..., width] in float32, float16 or bfloat16, parameters float32."""
+    """The block as a function; x [..., width] in float32, float16 or bfloat16 and of any strides, parameters float32."""
     for name, p in (("ln_w", ln_w), ("ln_b", ln_b), ("w1", w1), ("b1", b1), ("w2", w2), ("b2", b2)):
         if p.dtype != torch.float32:
             raise ValueError(f"{name} must be float32, got {p.dtype}")
-    rows = x.reshape(-1, x.shape[-1])
+    rows = x.reshape(-1, x.shape[-1])           # a view where there is one, of any strides
+    if (rows.shape[1] > 1 and rows.stride(1) != 1) or (rows.shape[0] > 1 and rows.stride(0) < rows.shape[1]):
+        rows = rows.contiguous()                 # the kernels take consecutive columns and rows that do not overlap
     return _MlpBlock.apply(rows, ln_w, ln_b, w1, b1, w2, b2, kind, eps).view(x.shape)
 
 
