@@ -197,7 +197,8 @@ constexpr int kBwdThreads = 512;
 // and db are summed per thread over its team's rows, joined over the block's teams, and
 // written as this block's row of `part`: [gridDim.x][2][pcols].
 //
-// Columns past the row's end load as zeros: their t is 0, and so is what they add to any sum.
+// Columns past the row's end load as zeros, and count from 0 instead of the mean: their t and xh are 0, and so is what
+// they add to any sum.  (-mean * rstd can pass the largest number, and 0 * Inf would reach the whole row.)
 template <typename T, typename W, bool CK, bool WHOLE, int TEAM, int NV>
 __global__ __launch_bounds__(kBwdThreads) void k_ln_backward(LnBwdArgs a, float* part, int64_t pcols) {
   constexpr int BT = kBwdThreads, RPB = BT / TEAM, TW = TEAM / kWave, SPAN = NV * TEAM * kChunk;
@@ -225,6 +226,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_backward(LnBwdArgs a, float*
   }
   __syncthreads();
   const auto weight = [&](int j, int h) { return s_w[(2 * j + h) * TEAM + lane]; };
+  const auto centre = [&](float mean, int j, int c) { return (WHOLE ? 0 : c) < n[j] ? mean : 0.0f; };   // of column c of chunk j
   const float cols = (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * RPB;
   struct Row {
@@ -275,7 +277,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_backward(LnBwdArgs a, float*
         cur.kept[j].half(h, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float xh = (x[i] - mean) * rstd, t = d[i] * w[i];
+          const float xh = (x[i] - centre(mean, j, 4 * h + i)) * rstd, t = d[i] * w[i];
           dw[j][4 * h + i] = __builtin_fmaf(d[i], xh, dw[j][4 * h + i]);
           db[j][4 * h + i] += d[i];
           s1 += t;
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_backward(LnBwdArgs a, float*
           get4<T>(cur.dy[j], h, d);
           cur.kept[j].half(h, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) out[4 * h + i] = rstd * __builtin_fmaf(-((x[i] - mean) * rstd), s2, __builtin_fmaf(d[i], w[i], -s1));
+          for (int i = 0; i < 4; ++i) out[4 * h + i] = rstd * __builtin_fmaf(-((x[i] - centre(mean, j, 4 * h + i)) * rstd), s2, __builtin_fmaf(d[i], w[i], -s1));
           if constexpr (!KEEP) __builtin_amdgcn_sched_barrier(0);
         }
         store8n<T, WHOLE>(static_cast<T*>(a.dx) + row * a.lddx + (int64_t)(lane + j * TEAM) * kChunk, n[j], out);

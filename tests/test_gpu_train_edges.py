@@ -66,3 +66,32 @@ def test_gelu_tail_is_as_exact_as_stated(gc):
     off = np.abs(host(gc.act_backward(torch.ones_like(x), "gelu", x=x)) - (p + s))
     bound = 1.01 * U * ((15 + 2.25 * v * v / 2) * p + (6 + 2.25 * v * v / 2) * np.abs(s) + np.abs(p + s))
     assert (off <= np.where(v < -13.2, np.abs(p + s), bound)).all()
+
+
+# --- layer norm -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+@pytest.mark.parametrize("cols", [1, 7, 96, 100, 600, 1025, 2056, 4095, 5000, 8200, 8201, 12300, 16001, 16390])
+def test_layernorm_backward_of_rows_far_from_zero(gc, name, cols):
+    """|mean| rstd past the largest fp32 number: the columns that exist have no deviation, so every xh is 0 and
+    dx = rstd (t - mean(t)); columns past the row's end add nothing.  Sums of t: a chain of at most 16 + 6 terms and
+    the team's, as rows / 8192 columns more for the widest; the result's own rounding on top."""
+    import torch
+    rows = 5
+    dt = getattr(torch, name)
+    x = torch.full((rows, cols), 2.0 ** 120, device="cuda", dtype=dt)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    dy = torch.randn(rows, cols, device="cuda", generator=g).to(dt)
+    mean = torch.full((rows,), 2.0 ** 120, device="cuda")
+    rstd = torch.full((rows,), 1e-5 ** -0.5, device="cuda")
+    t, r = host(dy), host(rstd)[0]
+    want = r * (t - t.mean(1, keepdims=True))
+    bound = r * (U * (50 * np.abs(t).mean(1, keepdims=True) + 8 * np.abs(t))) + torch.finfo(dt).eps / 2 * np.abs(want)
+    for kw in (dict(x=x), dict(ckpt=gc.ckpt_pack(x))):
+        dx, dw, db = gc.layernorm_backward(dy, mean, rstd, **kw)
+        assert (np.abs(host(dx) - want) <= bound).all(), list(kw)
+        assert not dw.any() and torch.isfinite(db).all()
+    # and the statistics themselves, where the sum of the row is a number
+    if cols < 256:
+        y, m, s, _, _ = gc.layernorm_forward(x)
+        assert not y.any() and torch.equal(m, mean) and np.abs(host(s) - r).max() <= 4 * U * r
