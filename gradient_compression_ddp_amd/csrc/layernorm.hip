@@ -374,28 +374,31 @@ __global__ __launch_bounds__(kBwdThreads) void k_ln_backward(LnBwdArgs a, float*
   }
 }
 
-// dw and db from the partial sums: 32 columns x 16 slices of the partials a block, each
+// dw and db from the partial sums: 32 columns x 16 slices of the partials a block at a time, each
 // slice summed in order, the slices then in order.
 constexpr int kSlices = 16;
 __global__ __launch_bounds__(32 * kSlices) void k_ln_join(const float* part, int parts, int64_t pcols, int64_t cols,
                                                  float* dw, float* db, int accumulate) {
   __shared__ float s[kSlices][32];
   const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;
   const int which = blockIdx.y;
-  float sum = 0.0f;
-  if (col < cols) {
-    const float* p = part + which * pcols + col;
-#pragma unroll 4
-    for (int i = slice; i < parts; i += kSlices) sum += p[(int64_t)i * 2 * pcols];
-  }
-  s[slice][c] = sum;
-  __syncthreads();
   float* out = which ? db : dw;
-  if (slice == 0 && col < cols && out) {
+  for (int64_t first = (int64_t)blockIdx.x * 32; first < cols; first += (int64_t)gridDim.x * 32) {
+    const int64_t col = first + c;
+    float sum = 0.0f;
+    if (col < cols) {
+      const float* p = part + which * pcols + col;
+#pragma unroll 4
+      for (int i = slice; i < parts; i += kSlices) sum += p[(int64_t)i * 2 * pcols];
+    }
+    s[slice][c] = sum;
+    __syncthreads();
+    if (slice == 0 && col < cols && out) {
 #pragma unroll
-    for (int i = 1; i < kSlices; ++i) sum += s[i][c];
-    out[col] = accumulate ? out[col] + sum : sum;
+      for (int i = 1; i < kSlices; ++i) sum += s[i][c];
+      out[col] = accumulate ? out[col] + sum : sum;
+    }
+    __syncthreads();
   }
 }
 
@@ -601,7 +604,9 @@ hipError_t backward_team(const LnBwdArgs& a, float* part, int64_t pcols, hipStre
 template <typename T, typename W, bool CK>
 hipError_t backward_ck(const LnBwdArgs& a, hipStream_t s) {
   const int64_t pcols = part_cols(a.cols);
-  const dim3 join((unsigned)ceil_div(a.cols, 32), 2);
+  // a dimension holds fewer than 2^32 threads: columns past 2^27 take further turns
+  const int64_t groups = ceil_div(a.cols, 32);
+  const dim3 join((unsigned)(groups < (int64_t(1) << 22) ? groups : (int64_t(1) << 22)), 2);
   if (a.rows == 0) {                       // nothing to sum: the sums are cleared
     k_ln_join<<<join, 32 * kSlices, 0, s>>>(nullptr, 0, pcols, a.cols, a.dw, a.db, a.accumulate);
     return hipGetLastError();

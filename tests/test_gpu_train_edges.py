@@ -95,3 +95,27 @@ def test_layernorm_backward_of_rows_far_from_zero(gc, name, cols):
     if cols < 256:
         y, m, s, _, _ = gc.layernorm_forward(x)
         assert not y.any() and torch.equal(m, mean) and np.abs(host(s) - r).max() <= 4 * U * r
+
+
+def test_layernorm_backward_of_the_widest_rows(gc):
+    """More columns than one launch has threads for: one row of 2^28 + 40, its far end included, and no rows."""
+    import torch
+    cols = 2 ** 28 + 40
+    none, st = torch.zeros(0, cols, device="cuda", dtype=torch.bfloat16), torch.zeros(0, device="cuda")
+    dw, db = torch.ones(cols, device="cuda"), torch.ones(cols, device="cuda")
+    gc.layernorm_backward(none, st, st, x=none, dw=dw, db=db)
+    assert not dw.any() and not db.any()
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(1, cols, device="cuda", generator=g).bfloat16()
+    dy = torch.randn(1, cols, device="cuda", generator=g).bfloat16()
+    mean, rstd = torch.full((1,), 0.25, device="cuda"), torch.full((1,), 1.5, device="cuda")
+    dx, dw, db = gc.layernorm_backward(dy, mean, rstd, x=x, dw=dw, db=db)
+    t = dy[0].double()
+    assert torch.equal(db.double(), t)                               # one row: the values themselves
+    xh = (x[0].double() - 0.25) * 1.5
+    assert ((dw.double() - t * xh).abs() <= 4 * U * (t * xh).abs()).all()
+    # a thread's chain of chunk sums: one per 8192 columns, its own and the team's 40 more; the two means enter every column
+    chain = (40 + cols / 8192) * U
+    want = 1.5 * (t - t.mean() - xh * (t * xh).mean())
+    off = (dx[0].double() - want).abs() - 2.0 ** -8 * want.abs()
+    assert (off <= 1.5 * (chain * (t.abs().mean() + xh.abs() * (t * xh).abs().mean()) + 16 * U * (t.abs() + xh.abs() + 1))).all()
