@@ -5,8 +5,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "gc.h"
 #include "internal.hpp"
+#include "overlap.hpp"
 #include "train_internal.hpp"
 
 namespace {
@@ -75,6 +78,30 @@ int check_weight_type(int dtype, int wdtype) {
   return GC_OK;
 }
 
+// What a call reads (out: false) and writes.  Threads read up to 8 elements that other threads write in a call on one
+// memory, so outputs in place of inputs are refused.
+struct Use {
+  const char* name;
+  gc::Area area;
+  bool out;
+};
+Use use(const char* name, bool out, const void* p, int64_t ld, int dtype, int64_t rows, int64_t cols) {
+  const int64_t s = elem_size(dtype);
+  return {name, {reinterpret_cast<uintptr_t>(p), cols * s, ld * s, rows}, out};
+}
+Use use_bytes(const char* name, bool out, const void* p, int64_t n) {
+  return {name, {reinterpret_cast<uintptr_t>(p), n, n, 1}, out};
+}
+int64_t codes_of(int64_t rows, int64_t cols) { return rows * ((cols + 31) / 32 * 32); }
+
+int check_apart(std::initializer_list<Use> uses) {
+  for (const Use* a = uses.begin(); a != uses.end(); ++a) {
+    for (const Use* b = a + 1; b != uses.end(); ++b)
+      GC_REQUIRE(!(a->out || b->out) || !gc::overlap(a->area, b->area), "%s and %s overlap", a->name, b->name);
+  }
+  return GC_OK;
+}
+
 bool f32_ok(const void* p) { return !p || aligned(p, 4); }
 
 hipStream_t to_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
@@ -89,6 +116,8 @@ int gc_ckpt_pack(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t co
   if (rows == 0 || cols == 0) return ok();
   GC_TRY(check_matrix("x", x, ldx, dtype, rows, cols));
   GC_TRY(check_ckpt("x", codes, exps, rows, cols));
+  GC_TRY(check_apart({use("x", false, x, ldx, dtype, rows, cols), use_bytes("codes", true, codes, codes_of(rows, cols)),
+                      use_bytes("exponents", true, exps, codes_of(rows, cols) / 32)}));
   gc::ActFwdArgs a{};
   a.x = x; a.ldx = ldx; a.rows = rows; a.cols = cols;
   a.x_codes = codes; a.x_exps = exps;
@@ -101,6 +130,8 @@ int gc_ckpt_unpack(int dtype, const int8_t* codes, const uint8_t* exps, int64_t 
   if (rows == 0 || cols == 0) return ok();
   GC_TRY(check_ckpt("the checkpoint's", codes, exps, rows, cols));
   GC_TRY(check_matrix("out", out, ldo, dtype, rows, cols));
+  GC_TRY(check_apart({use_bytes("codes", false, codes, codes_of(rows, cols)), use("out", true, out, ldo, dtype, rows, cols),
+                      use_bytes("exponents", false, exps, codes_of(rows, cols) / 32)}));
   gc::ActBwdArgs a{};
   a.x_codes = codes; a.x_exps = exps; a.rows = rows; a.cols = cols;
   a.dx = out; a.lddx = ldo;
@@ -116,6 +147,9 @@ int gc_act_forward(int dtype, int kind, const void* x, int64_t ldx, int64_t rows
   GC_TRY(check_matrix("y", y, ldy, dtype, rows, cols));
   GC_TRY(check_pack("x", x_codes, x_exps, rows, cols));
   GC_TRY(check_pack("y", y_codes, y_exps, rows, cols));
+  GC_TRY(check_apart({use("x", false, x, ldx, dtype, rows, cols), use("y", true, y, ldy, dtype, rows, cols),
+                      use_bytes("x's codes", true, x_codes, codes_of(rows, cols)), use_bytes("x's exponents", true, x_exps, codes_of(rows, cols) / 32),
+                      use_bytes("y's codes", true, y_codes, codes_of(rows, cols)), use_bytes("y's exponents", true, y_exps, codes_of(rows, cols) / 32)}));
   gc::ActFwdArgs a{};
   a.x = x; a.ldx = ldx; a.rows = rows; a.cols = cols; a.y = y; a.ldy = ldy;
   a.x_codes = x_codes; a.x_exps = x_exps; a.y_codes = y_codes; a.y_exps = y_exps;
@@ -132,6 +166,9 @@ int gc_act_backward(int dtype, int kind, const void* dy, int64_t lddy, const voi
   if (x) GC_TRY(check_matrix("x", x, ldx, dtype, rows, cols));
   else GC_TRY(check_ckpt("x", x_codes, x_exps, rows, cols));
   GC_TRY(check_matrix("dx", dx, lddx, dtype, rows, cols));
+  GC_TRY(check_apart({use("dy", false, dy, lddy, dtype, rows, cols), use("dx", true, dx, lddx, dtype, rows, cols),
+                      use("x", false, x, ldx, dtype, rows, cols),
+                      use_bytes("codes", false, x_codes, codes_of(rows, cols)), use_bytes("exponents", false, x_exps, codes_of(rows, cols) / 32)}));
   gc::ActBwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.x = x; a.ldx = ldx; a.x_codes = x_codes; a.x_exps = x_exps;
   a.rows = rows; a.cols = cols; a.dx = dx; a.lddx = lddx;
@@ -153,6 +190,11 @@ int gc_layernorm_forward(int dtype, const void* x, int64_t ldx, int64_t rows, in
   GC_REQUIRE(mean && rstd && f32_ok(mean) && f32_ok(rstd), "mean and rstd must be non-NULL and 4-byte aligned");
   GC_TRY(check_pack("x", x_codes, x_exps, rows, cols));
   GC_TRY(check_pack("y", y_codes, y_exps, rows, cols));
+  GC_TRY(check_apart({use("x", false, x, ldx, dtype, rows, cols), use("y", true, y, ldy, dtype, rows, cols),
+                      use("weight", false, weight, cols, wdtype, 1, cols), use("bias", false, bias, cols, wdtype, 1, cols),
+                      use_bytes("mean", true, mean, rows * 4), use_bytes("rstd", true, rstd, rows * 4),
+                      use_bytes("x's codes", true, x_codes, codes_of(rows, cols)), use_bytes("x's exponents", true, x_exps, codes_of(rows, cols) / 32),
+                      use_bytes("y's codes", true, y_codes, codes_of(rows, cols)), use_bytes("y's exponents", true, y_exps, codes_of(rows, cols) / 32)}));
   gc::LnFwdArgs a{};
   a.x = x; a.ldx = ldx; a.rows = rows; a.cols = cols; a.w = weight; a.b = bias; a.eps = eps; a.y = y; a.ldy = ldy;
   a.mean = mean; a.rstd = rstd;
@@ -189,7 +231,14 @@ int gc_layernorm_backward(int dtype, const void* dy, int64_t lddy, const void* x
   GC_REQUIRE(aligned(weight, (size_t)elem_size(wdtype)), "weight must be aligned to its element");
   GC_REQUIRE(mean && rstd && f32_ok(mean) && f32_ok(rstd), "mean and rstd must be non-NULL and 4-byte aligned");
   GC_TRY(check_matrix("dx", dx, lddx, dtype, rows, cols));
-  GC_TRY(check_workspace(workspace, workspace_bytes, gc::layernorm_backward_workspace(rows, cols)));
+  const size_t need = gc::layernorm_backward_workspace(rows, cols);
+  GC_TRY(check_workspace(workspace, workspace_bytes, need));
+  GC_TRY(check_apart({use("dy", false, dy, lddy, dtype, rows, cols), use("dx", true, dx, lddx, dtype, rows, cols),
+                      use("x", false, x, ldx, dtype, rows, cols),
+                      use_bytes("codes", false, x_codes, codes_of(rows, cols)), use_bytes("exponents", false, x_exps, codes_of(rows, cols) / 32),
+                      use("weight", false, weight, cols, wdtype, 1, cols), use_bytes("mean", false, mean, rows * 4),
+                      use_bytes("rstd", false, rstd, rows * 4), use_bytes("dw", true, dw, cols * 4), use_bytes("db", true, db, cols * 4),
+                      use_bytes("workspace", true, workspace, (int64_t)need)}));
   a.dy = dy; a.lddy = lddy; a.x = x; a.ldx = ldx; a.x_codes = x_codes; a.x_exps = x_exps; a.w = weight;
   a.mean = mean; a.rstd = rstd; a.dx = dx; a.lddx = lddx; a.ws = workspace;
   return launched(gc::launch_layernorm_backward(dtype, wdtype, a, to_stream(stream)), "gc_layernorm_backward");
@@ -224,7 +273,12 @@ int gc_linear_wgrad(int dtype, const void* dy, int64_t lddy, const int8_t* codes
   }
   GC_TRY(check_matrix("dy", dy, lddy, dtype, rows, out_features));
   GC_TRY(check_ckpt("the checkpoint's", codes, exps, rows, in_features));
-  GC_TRY(check_workspace(workspace, workspace_bytes, gc::wgrad_workspace(dtype, rows, in_features, out_features)));
+  const size_t need = gc::wgrad_workspace(dtype, rows, in_features, out_features);
+  GC_TRY(check_workspace(workspace, workspace_bytes, need));
+  GC_TRY(check_apart({use("dy", false, dy, lddy, dtype, rows, out_features), use("dw", true, dw, lddw, GC_F32, out_features, in_features),
+                      use_bytes("codes", false, codes, codes_of(rows, in_features)),
+                      use_bytes("exponents", false, exps, codes_of(rows, in_features) / 32), use_bytes("db", true, db, out_features * 4),
+                      use_bytes("workspace", true, workspace, (int64_t)need)}));
   a.dy = dy; a.lddy = lddy; a.codes = codes; a.exps = exps; a.ws = workspace;
   return launched(gc::launch_wgrad(dtype, a, to_stream(stream)), "gc_linear_wgrad");
 }

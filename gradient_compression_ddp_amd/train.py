@@ -7,7 +7,8 @@ pointers and the HIP stream to the C ABI.
 
 Matrices are 2-D tensors with consecutive columns (``stride(1) == 1``) and any row stride.
 A checkpoint is a pair of tensors ``(codes, exps)``: int8 [rows, 32 * ceil(cols / 32)] and
-uint8 [rows, ceil(cols / 32)], both contiguous.
+uint8 [rows, ceil(cols / 32)], both contiguous.  Outputs that a caller passes may not overlap the inputs or
+each other (no call works in place); one that does raises GCError.
 
 ``stream``: the torch stream to enqueue on, by default the current one.  With another
 stream, what a call allocates belongs to that stream's pool and the tensors passed in are

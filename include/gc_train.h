@@ -7,7 +7,8 @@
  * Conventions for every call
  *   - As in gc.h: device pointers, work only enqueued on `stream` (a hipStream_t as void*),
  *     nothing synchronized, allocated or read back; the caller owns every buffer and the
- *     workspace; outputs must not overlap inputs or each other; arguments are checked on the
+ *     workspace; outputs that overlap inputs or each other are refused (slices beside each
+ *     other of one wider matrix do not overlap); arguments are checked on the
  *     host before anything is enqueued and a rejected call makes no HIP call (gc_last_error()
  *     has the reason).
  *   - A matrix is rows x cols of one element type (enum gc_dtype) with consecutive columns; a

@@ -119,3 +119,42 @@ def test_layernorm_backward_of_the_widest_rows(gc):
     want = 1.5 * (t - t.mean() - xh * (t * xh).mean())
     off = (dx[0].double() - want).abs() - 2.0 ** -8 * want.abs()
     assert (off <= 1.5 * (chain * (t.abs().mean() + xh.abs() * (t * xh).abs().mean()) + 16 * U * (t.abs() + xh.abs() + 1))).all()
+
+
+# --- outputs and inputs in one memory ---------------------------------------------------------
+
+def test_slices_beside_each_other(gc):
+    """Every operand a run of columns of one wider matrix: the same bits as apart."""
+    import torch
+    rows, cols = 37, 101
+    wide = torch.randn(rows, 4 * cols + 3, device="cuda").bfloat16()
+    x, dy, y, dx = (wide[:, k * cols + 1:(k + 1) * cols + 1] for k in range(4))
+    xa, dya = x.clone(), dy.clone()
+    w = torch.rand(cols, device="cuda")
+    edge = wide[:, [0, -2, -1]].clone()
+    gc.act_forward(x, "silu", y=y)
+    assert torch.equal(y, gc.act_forward(xa, "silu")[0])
+    gc.act_backward(dy, "silu", x=x, dx=dx)
+    assert torch.equal(dx, gc.act_backward(dya, "silu", x=xa))
+    _, mean, rstd, _, _ = gc.layernorm_forward(x, w, y=y)
+    assert torch.equal(y, gc.layernorm_forward(xa, w)[0])
+    gc.layernorm_backward(dy, mean, rstd, w, x=x, dx=dx)
+    assert torch.equal(dx, gc.layernorm_backward(dya, mean, rstd, w, x=xa)[0])
+    assert torch.equal(x, xa) and torch.equal(dy, dya) and torch.equal(wide[:, [0, -2, -1]], edge)
+
+
+def test_in_place_is_refused(gc):
+    import torch
+    x = torch.randn(37, 101, device="cuda")
+    dy, w = torch.randn_like(x), torch.rand(101, device="cuda")
+    _, mean, rstd, ckpt, _ = gc.layernorm_forward(x, pack_x=True)
+    wide = torch.randn(37, 150, device="cuda")
+    was = [t.clone() for t in (x, dy, wide)]
+    for call in (lambda: gc.act_forward(x, y=x), lambda: gc.act_backward(dy, x=x, dx=dy), lambda: gc.act_backward(dy, x=x, dx=x),
+                 lambda: gc.act_forward(wide[:, :101], y=wide[:, 49:]), lambda: gc.layernorm_forward(x, y=x),
+                 lambda: gc.layernorm_backward(dy, mean, rstd, x=x, dx=dy), lambda: gc.layernorm_backward(dy, mean, rstd, ckpt=ckpt, dx=dy),
+                 lambda: gc.layernorm_backward(dy, mean, rstd, w, x=x, dw=w), lambda: gc.layernorm_backward(dy, mean, rstd, x=x, dw=w, db=w),
+                 lambda: gc.linear_wgrad(x[:, :30], *ckpt, 101, dw=x[:30])):
+        with pytest.raises(gc.GCError, match="overlap"):
+            call()
+    assert all(torch.equal(a, b) for a, b in zip((x, dy, wide), was))
