@@ -158,3 +158,91 @@ def test_in_place_is_refused(gc):
         with pytest.raises(gc.GCError, match="overlap"):
             call()
     assert all(torch.equal(a, b) for a, b in zip((x, dy, wide), was))
+
+
+# --- more rows than blocks, and rows that are not numbers -------------------------------------
+
+# The forward pass gives a block a second row past 8192 rows (teams of 64 threads), 2048 (256) or 1024 (512); the backward
+# pass a second and third one past 256 blocks, with several partial sums to join.  Whole and ragged widths of each team.
+WALKS = [(8300, 100), (8300, 520), (2100, 1032), (2100, 2049), (2100, 4096), (1100, 8192), (1100, 8201), (1100, 12296), (1100, 16383),
+         (600, 16384), (40, 16385)]
+
+
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols", WALKS)
+def test_layernorm_row_walk(gc, name, rows, cols):
+    """Bounds as for one row a block: a thread's chain of at most 16 terms (one more per 8192 columns) and the team's tree."""
+    import torch
+    dt = getattr(torch, name)
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    x = (rand(rows, cols) * torch.exp(0.5 * rand(cols)) + 0.3 * rand(rows, 1)).to(dt)
+    dy = (rand(rows, cols) * rand(rows, 1).abs()).to(dt)
+    w, b = 1 + 0.2 * rand(cols), 0.1 * rand(cols)
+    y, mean, rstd, xc, yc = gc.layernorm_forward(x, w, b, pack_x=True, pack_y=True)
+    # row by row the same as in calls that give every row a team of its own
+    some = 500
+    for r in range(0, rows, some):
+        part = gc.layernorm_forward(x[r:r + some], w, b, pack_x=True, pack_y=True)
+        assert torch.equal(part[0], y[r:r + some]) and torch.equal(part[1], mean[r:r + some]) and torch.equal(part[2], rstd[r:r + some])
+        for p, q in ((part[3], xc), (part[4], yc)):
+            assert torch.equal(p[0], q[0][r:r + some]) and torch.equal(p[1], q[1][r:r + some])
+    again = gc.layernorm_forward(x, w, b, pack_x=True, pack_y=True)
+    assert all(torch.equal(p, q) for p, q in zip(again[:3], (y, mean, rstd)))
+    xv, half = x.double(), torch.finfo(dt).eps / 2
+    m = xv.mean(1)
+    r = 1 / torch.sqrt((xv - m[:, None]).square().mean(1) + 1e-5)
+    chain = 40 + cols / 8192
+    dm = chain * U * xv.abs().mean(1) + U * m.abs()
+    dr = 0.5 * (2 * chain * U + (dm * r) ** 2) + 4 * U
+    assert ((mean.double() - m).abs() <= dm + U * m.abs()).all() and ((rstd.double() - r).abs() <= (dr + U) * r).all()
+    xh = (xv - m[:, None]) * r[:, None]
+    want = xh * w.double() + b.double()
+    bound = w.double().abs() * ((dm * r)[:, None] + xh.abs() * (dr[:, None] + 4 * U)) + (4 * U + half) * want.abs()
+    assert ((y.double() - want).abs() <= bound).all()
+    # backward, from the statistics as stored
+    m, r, dv, wv = mean.double()[:, None], rstd.double()[:, None], dy.double(), w.double()
+    for kw, kept in ((dict(ckpt=xc), gc.ckpt_unpack(*xc, cols, dt).double()), (dict(x=x), xv)):
+        dx, dw, db = gc.layernorm_backward(dy, mean, rstd, w, **kw)
+        xh, t = (kept - m) * r, dv * wv
+        want = r * (t - t.mean(1, keepdim=True) - xh * (t * xh).mean(1, keepdim=True))
+        bound = r * U * (8 * t.abs() + (chain + 8) * t.abs().mean(1, keepdim=True) + (chain + 16) * xh.abs() * (t * xh).abs().mean(1, keepdim=True))
+        assert ((dx.double() - want).abs() <= bound + half * want.abs()).all(), list(kw)
+        assert ((dw.double() - (dv * xh).sum(0)).abs() <= (rows + 8) * U * (dv * xh).abs().sum(0)).all(), list(kw)
+        assert ((db.double() - dv.sum(0)).abs() <= rows * U * dv.abs().sum(0)).all(), list(kw)
+        for _ in range(3):
+            assert all(torch.equal(p, q) for p, q in zip(gc.layernorm_backward(dy, mean, rstd, w, **kw), (dx, dw, db)))
+
+
+@pytest.mark.parametrize("name", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("cols", [5, 100, 512, 2049, 4096, 9000, 16390])
+def test_layernorm_non_finite_rows(gc, name, cols):
+    """A row with an Inf or a NaN has no finite statistics, result or dx, and dw none where it enters; every other
+    row, and db, are as without it.  An Inf of dy stays in its row of dx and its column of dw and db."""
+    import torch
+    dt = getattr(torch, name)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    rows, bad = 23, [3, 7, 22]
+    x, dy = (torch.randn(rows, cols, device="cuda", generator=g).to(dt) for _ in range(2))
+    w, b = torch.rand(cols, device="cuda", generator=g) + 0.5, torch.rand(cols, device="cuda", generator=g)
+    fine = [i for i in range(rows) if i not in bad]
+    odd = x.clone()
+    for i, v in zip(bad, ("inf", "nan", "-inf")):
+        odd[i, (i * 37) % cols] = float(v)
+    want, got = (gc.layernorm_forward(v, w, b, pack_x=True) for v in (x, odd))
+    assert got[0][bad].isnan().all() and got[2][bad].isnan().all() and not torch.isfinite(got[1][bad]).any()
+    for p, q in zip(got[:3], want):
+        assert torch.equal(p[fine], q[fine])
+    for kw, kw_odd in ((dict(x=x), dict(x=odd)), (dict(ckpt=want[3]), dict(ckpt=got[3]))):
+        dx, dw, db = gc.layernorm_backward(dy, want[1], want[2], w, **kw)
+        dx2, dw2, db2 = gc.layernorm_backward(dy, got[1], got[2], w, **kw_odd)
+        assert torch.equal(dx2[fine], dx[fine]) and dx2[bad].isnan().all()
+        assert torch.equal(db2, db) and dw2.isnan().all()
+        c = 11 % cols
+        far = dy.clone()
+        far[9, c] = float("inf")
+        dx3, dw3, db3 = gc.layernorm_backward(far, want[1], want[2], w, **kw)
+        rest, cut = [i for i in range(rows) if i != 9], [i for i in range(cols) if i != c]
+        assert torch.equal(dx3[rest], dx[rest]) and not torch.isfinite(dx3[9]).any()
+        assert torch.equal(dw3[cut], dw[cut]) and torch.equal(db3[cut], db[cut])
+        assert db3[c] == float("inf") and not torch.isfinite(dw3[c])
