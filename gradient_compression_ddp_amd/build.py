@@ -3,11 +3,14 @@
 Flags: -O3, -ffp-contract=off (no fused multiply-add, so every float operation rounds
 once, as the numeric contract requires), IEEE division and square root (hipcc's default),
 denormals kept (the default on gfx950), and packed-fp32 instruction selection turned off.
+No kernel may use scratch memory: the build fails if one does (layer norm teams of 1024 threads that
+spilled their registers there gave sums that differed from run to run).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -32,6 +35,7 @@ COMMON_FLAGS = [
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-fno-gpu-rdc",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-Rpass-analysis=kernel-resource-usage",
 ]
 
 
@@ -42,8 +46,19 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the HIP toolchain is required to build libgc.so")
 
 
-def _compile(src: str, verbose: bool) -> str:
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+def scratch_users(remarks: str) -> dict:
+    """{kernel: bytes of scratch a lane} of the kernels that use any, from the compiler's resource remarks."""
+    found, name = {}, "?"
+    for key, value in re.findall(r"remark:\s+(Function Name|ScratchSize \[bytes/lane\]): (\S+)", remarks):
+        if key == "Function Name":
+            name = value
+        elif value != "0":
+            found[name] = int(value)
+    return found
+
+
+def _compile(src: str, verbose: bool, obj: str = None) -> str:
+    obj = obj or os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     hip = src.endswith(".hip")
     # the language flag must come before the source it applies to
     cmd = [hipcc()] + (["-x", "hip"] if hip else []) + ["-c", os.path.join(CSRC, src), "-o", obj] + COMMON_FLAGS
@@ -54,8 +69,15 @@ def _compile(src: str, verbose: bool) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"compiling {src} failed:\n{res.stdout}\n{res.stderr}")
-    if res.stderr.strip() and verbose:
-        print(res.stderr, file=sys.stderr)
+    scratch = scratch_users(res.stderr)
+    if scratch:
+        os.remove(obj)
+        raise RuntimeError(f"{src}: kernels use scratch memory: {scratch}")
+    if verbose:
+        # the remarks, and the source lines printed under them, are not for reading
+        rest = [line for line in res.stderr.splitlines() if ": remark:" not in line and not re.match(r"\s*\d* \|", line)]
+        if rest:
+            print("\n".join(rest), file=sys.stderr)
     return obj
 
 
