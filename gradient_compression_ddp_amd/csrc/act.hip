@@ -31,8 +31,9 @@ constexpr int kNone = -1;
 // x Q(z) and f', which are below 2^-122 there, are 0.
 //
 // The tanh form is x * p with p = 1 / (1 + exp(-u)), u = 2 sqrt(2/pi) (x + 0.044715 x^3), and
-// f' = p + x p (1 - p) u'.  Past |x| = 32, p is 0 or 1 and p (1 - p) is 0 in fp32, so x is limited there before
-// its cube can overflow.  SiLU is x * p with u = x, f' = p (1 + x (1 - p)).
+// f' = p + x p (1 - p) u'.  Past |x| = 11.5, p is 0 or 1 and p (1 - p) is 0 in fp32, so x is limited there before
+// its cube can overflow.  SiLU is x * p with u = x, f' = p (1 + x (1 - p)); the limit there is 131.  Limits drop a NaN:
+// x itself is a factor of the results.
 // ---------------------------------------------------------------------------------
 __device__ __forceinline__ float exp2_hw(float a) { return __builtin_amdgcn_exp2f(a); }
 __device__ __forceinline__ float rcp_hw(float a) { return __builtin_amdgcn_rcpf(a); }
@@ -56,13 +57,21 @@ constexpr float kLog2e = 1.44269504f;
 // 1 / (1 + exp(-u)).  The hardware's exp2 and reciprocal flush results below 2^-126, where f' still multiplies p by some
 // hundreds: far out they work on 2^-64 (1 + exp(-u)) instead, and the last product, which does not flush, scales back.
 // Only there: the shift rounds the exponent at its own size of 64, 2e-6 of p, where u itself is small (p was
-// off by up to 1.4e-6 for |u| < 1 with the shift everywhere, and is by 1.2e-7 now).  Past -40 the shifted
+// off by up to 1.4e-6 for |u| < 1 with the shift everywhere).  Past -40 the shifted
 // exponent is the smaller one.
+//
+// The reciprocal is corrected once, which leaves it off by about half a step instead of a whole one: with the
+// hardware's own, SiLU of 5.9375 in bf16, 1.6 units of 2^-24 from the middle between two results, came out as the other
+// one.  The correction must meet no Inf: u is at least -131, where p is 0 already.
 __device__ __forceinline__ float sigmoid(float u) {
   const bool far = u < -40.0f;
   const float k = far ? 5.42101086e-20f : 1.0f;              // 2^-64
-  return k * rcp_hw(k + exp2_hw(__builtin_fmaf(u, -kLog2e, far ? -64.0f : 0.0f)));
+  const float d = k + exp2_hw(__builtin_fmaf(u, -kLog2e, far ? -64.0f : 0.0f));
+  const float r = rcp_hw(d);
+  return k * __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
+
+__device__ __forceinline__ float silu_arg(float x) { return __builtin_amdgcn_fmed3f(x, -131.0f, 131.0f); }
 
 template <int KIND>
 __device__ __forceinline__ float act_f(float x) {
@@ -71,11 +80,11 @@ __device__ __forceinline__ float act_f(float x) {
     const float q = gelu_tail(z, exp2_hw(z * z * (-0.5f * kLog2e)));
     return x * (x < 0.0f ? q : 1.0f - q);
   } else if constexpr (KIND == GC_ACT_GELU_TANH) {
-    const float c = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f);
+    const float c = __builtin_amdgcn_fmed3f(x, -11.5f, 11.5f);
     const float u = c * __builtin_fmaf(c * c, 2.0f * 0.79788456f * 0.044715f, 2.0f * 0.79788456f);
     return x * sigmoid(u);
   } else {
-    return x * sigmoid(x);
+    return x * sigmoid(silu_arg(x));
   }
 }
 
@@ -87,7 +96,7 @@ __device__ __forceinline__ float act_d(float x) {
     const float q = gelu_tail(z, e);
     return __builtin_fmaf(x, e * 0.39894228f, x < 0.0f ? q : 1.0f - q);
   } else if constexpr (KIND == GC_ACT_GELU_TANH) {
-    const float c = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f);
+    const float c = __builtin_amdgcn_fmed3f(x, -11.5f, 11.5f);
     const float c2 = c * c;
     const float u = c * __builtin_fmaf(c2, 2.0f * 0.79788456f * 0.044715f, 2.0f * 0.79788456f);
     const float du = __builtin_fmaf(c2, 6.0f * 0.79788456f * 0.044715f, 2.0f * 0.79788456f);
@@ -95,7 +104,7 @@ __device__ __forceinline__ float act_d(float x) {
     const float d = __builtin_fmaf(c * du, p * (1.0f - p), p);
     return x != x ? x : d;          // the limit above drops a NaN
   } else {
-    const float p = sigmoid(x);
+    const float p = sigmoid(silu_arg(x));
     return p * __builtin_fmaf(x, 1.0f - p, 1.0f);
   }
 }

@@ -68,6 +68,20 @@ def test_gelu_tail_is_as_exact_as_stated(gc):
     assert (off <= np.where(v < -13.2, np.abs(p + s), bound)).all()
 
 
+@pytest.mark.parametrize("kind", ["gelu", "gelu_tanh", "silu"])
+def test_every_bf16_value(gc, kind):
+    """All finite bfloat16 inputs: the result is the 64-bit one's nearest bfloat16, wherever it is above the flushed tail."""
+    import torch
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = x[torch.isfinite(x)][None]
+    want = torch.from_numpy(o.act_forward(x.double().numpy(), kind))
+    got = gc.act_forward(x.cuda(), kind)[0].cpu()
+    off = (got != want.bfloat16()) & (want.abs() >= 2.0 ** -100)
+    assert not off.any(), (x[off].tolist(), want[off].tolist(), got[off].tolist())
+    tail = want.abs() < 2.0 ** -100
+    assert (got[tail].double() - want[tail]).abs().max() < 2.0 ** -99
+
+
 # --- layer norm -----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("name", ["float32", "bfloat16"])
