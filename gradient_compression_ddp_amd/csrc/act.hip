@@ -2,10 +2,12 @@
 // around it (gc_ckpt_pack, gc_ckpt_unpack, gc_act_forward, gc_act_backward).
 //
 // All four are one pass over the matrix in chunks of 8 columns (ckpt_core.hpp), bound by HBM; two chunks of a
-// thread are in flight at a time.  Measured over 8192 x 11008 in bf16, inputs outside the caches (a copy of
-// that size: 5.3 TB/s): pack 43 us, 6.3 TB/s; unpack 43 us, 6.4 TB/s; the GELU forward with x packed 82 us, 5.6 TB/s, with
-// x and y packed 103 us, 5.3 TB/s; its backward from the checkpoint 82 us, 5.5 TB/s.  Rows of 1000 in fp16 (no multiple
-// of 32, so with ragged ends): 3.8 to 5 TB/s.  Small calls are a launch: 2.5 to 4 us on the card.
+// thread are in flight at a time.  Measured over 8192 x 11008 in bf16, one call repeated on three sets of inputs (a copy of
+// that size: 5.3 TB/s): pack 43 us, 6.4 TB/s; unpack 43 us, 6.3 TB/s; the GELU forward with x packed 79 to 87 us, 5.2 to 5.7
+// TB/s, with x and y packed 98 us, 5.6 TB/s; its backward from the checkpoint 79 us, 5.7 TB/s, from x 95 us, 5.7 TB/s.  SiLU
+// and tanh-GELU take 79 to 80 us both ways; fp32 takes 143 to 146 us, and 184 us back from x.  (Pack and unpack in turn take 52
+// and 39: the one writes back what the other left in the last-level cache, the other reads its checkpoint there.)  Rows of 1000
+// in fp16 (no multiple of 32, so with ragged ends): 3.8 to 5 TB/s.  Small calls are a launch: 2.5 to 4 us on the card.
 #include <hip/hip_runtime.h>
 
 #include "ckpt_core.hpp"

@@ -10,10 +10,11 @@
 // 16-bit types half the registers of its fp32 values.
 // Wider rows take the looped kernels at the end of this file, which re-read the row.
 //
-// Bound by HBM.  Measured over 16384 x 4096 in bf16, inputs outside the caches (a copy of that size: 6.0 TB/s):
-// forward 47 us, 5.7 TB/s; with x packed 66 us, 5.1 TB/s; backward with dw and db from the checkpoint 78 us, 4.4 TB/s,
-// from x 79 us, 5.1 TB/s.  The backward pass falls short of the copy by its two row sums, a barrier each row, and by
-// joining dw and db (5 us).  Rows of 20000 (looped): 2.5 to 3.0 TB/s of bytes counted once.
+// Bound by HBM.  Measured over 16384 x 4096 in bf16, one call repeated on four sets of inputs (a copy of that size: 5.3
+// TB/s): forward 46 us, 5.8 TB/s; with x packed 66 us, 5.1 TB/s; backward with dw and db from the checkpoint 67 to 75 us, 4.5
+// to 5.0 TB/s, from x 80 us, 5.0 TB/s.  The backward pass falls short of the copy by its two row sums, a barrier each row, and
+// by joining dw and db (5 us).  Rows of 20000 (looped), 4096 of them: forward 116 us, backward 157 from the checkpoint and 180
+// from x, 2.6 to 2.8 TB/s of bytes counted once, since they read the row three times and twice.
 //
 // Statistics: mean first, then the sum of squared deviations from it, both over registers,
 // so nothing cancels when the mean is large against the deviation.

@@ -13,14 +13,17 @@
 // accumulation.  An fp32 dy is cut into three bf16 parts whose sum is dy (8 significant bits each, down to 2^-133): three
 // matrix instructions at the bf16 rate instead of one at the fp32 rate, which is a sixteenth of it.
 //
-// Measured, with db (fastest of repeated calls, 8-bit checkpoint of the same type):
-//   bf16  rows 4096, 4096 x 4096:   123 us, 1117 TFLOP/s      rows 8192, 11008 x 4096:  664 us, 1112 TFLOP/s
-//   fp32  rows 4096, 4096 x 4096:   355 us,  387 TFLOP/s (1160 of bf16 products)
+// Measured, with db (fastest of repeated calls, 8-bit checkpoint of the same type; the range is that of several cards):
+//   bf16  rows 4096, 4096 x 4096:   123 to 131 us, 1050 to 1120 TFLOP/s      rows 8192, 11008 x 4096:  642 to 683 us, 1080 to 1150 TFLOP/s
+//   fp32  rows 4096, 4096 x 4096:   335 to 355 us,  390 to 410 TFLOP/s (three times that of bf16 products)
 //   bf16  rows 32, 1024 x 1024:     10 us, a launch and its call      fp32  rows 1000, 1333 x 999:  29 us
-// Large products are bound by the issue of the inner loop at the clock that the card holds under it (about 2.1 GHz of 2.4):
-// half of the matrix cycles are used (the one wave of a SIMD issues about eight other instructions beside each product,
-// and LDS moves 96 KB a stage), all-zero inputs run 15% faster for their power alone, and inputs that stay in the
-// caches 5% faster.  Small ones are bound by the latency of a stage's loads and by storing the shares' sums.
+// Added to what is there, the first two take 187 and 933 us: every row of a wave's tile waits for its own read.
+// Large products use half of the matrix cycles, at the clock that the card holds under them (about 2.1 GHz of 2.4).  By the
+// counters, of the time of the one wave of a SIMD, products take 58%; for 19% it waits for memory, LDS or the barrier, and for 27% it
+// has an instruction that does not issue, partly behind a product.  Beside each product it issues 2.6 vector, 1.25 LDS and one
+// other instruction.  LDS is not the limit by its rate: it is active in a quarter of the cycles, without bank conflicts.
+// All-zero inputs run 15% faster for their power alone, and inputs that stay in the caches 5% faster.  Small
+// products are bound by the latency of a stage's loads and by storing the shares' sums.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_wgrad(WgradArgs a, TileMap map,
 // matrix cores' time.  With one wave per SIMD nothing else fills a stall, so the order of the instructions is
 // fixed by hand (the compiler's own order took 151 us, not 123, for 4096 rows of 4096 x 4096, and 256 x 128 tiles with
 // two blocks per CU 158): a stage of 32 rows is two halves of 16 slots of one 32 x 32 x 16 product (32 cycles),
-// and every slot carries a share of the rest (about six instructions, four cycles each).
+// and every slot carries a share of the rest (about five instructions, four cycles each).
 //
 // fp32: 128 outputs x 256 inputs, 24 slots a half, since each product of a pair of tiles is three (one per
 // plane of dy); the cutting of dy into planes is part of the slots' other work.

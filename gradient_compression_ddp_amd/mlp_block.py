@@ -10,8 +10,9 @@ the activation and the two weight-gradient calls are the library's kernels (gc_t
 W2 are torch's.
 
 Parameters are float32 (what the compressors and the optimizer work on) and are cast to
-the input's type for the products.  Their gradients come out in float32; with ``.grad`` preset to
-views of a flat bucket, autograd adds into the bucket that the compressors take.
+the input's type for the products.  Their gradients come out in float32, in memory of their own; with ``.grad`` preset to
+views of a flat bucket, autograd adds them into the bucket that the compressors take (a caller of
+:func:`~.train.linear_wgrad` can have the kernel add into the bucket itself).
 """
 from __future__ import annotations
 
