@@ -34,8 +34,8 @@ constexpr int kNone = -1;
 //
 // The tanh form is x * p with p = 1 / (1 + exp(-u)), u = 2 sqrt(2/pi) (x + 0.044715 x^3), and
 // f' = p + x p (1 - p) u'.  Past |x| = 11.5, p is 0 or 1 and p (1 - p) is 0 in fp32, so x is limited there before
-// its cube can overflow.  SiLU is x * p with u = x, f' = p (1 + x (1 - p)); the limit there is 131.  Limits drop a NaN:
-// x itself is a factor of the results.
+// its cube can overflow.  SiLU is x * p with u = x, f' = p (1 + x (1 - p)); the limit there is 131.  A limit drops a NaN,
+// which comes back with the factor x, or by a test.
 // ---------------------------------------------------------------------------------
 __device__ __forceinline__ float exp2_hw(float a) { return __builtin_amdgcn_exp2f(a); }
 __device__ __forceinline__ float rcp_hw(float a) { return __builtin_amdgcn_rcpf(a); }
@@ -62,9 +62,9 @@ constexpr float kLog2e = 1.44269504f;
 // off by up to 1.4e-6 for |u| < 1 with the shift everywhere).  Past -40 the shifted
 // exponent is the smaller one.
 //
-// The reciprocal is corrected once, which leaves it off by about half a step instead of a whole one: with the
+// The reciprocal takes one Newton step, which leaves it off by about half a step instead of a whole one: with the
 // hardware's own, SiLU of 5.9375 in bf16, 1.6 units of 2^-24 from the middle between two results, came out as the other
-// one.  The correction must meet no Inf: u is at least -131, where p is 0 already.
+// one.  The step must meet no Inf: u is at least -131, where p is 0 already.
 __device__ __forceinline__ float sigmoid(float u) {
   const bool far = u < -40.0f;
   const float k = far ? 5.42101086e-20f : 1.0f;              // 2^-64
