@@ -14,7 +14,7 @@
 // matrix instructions at the bf16 rate instead of one at the fp32 rate, which is a sixteenth of it.
 //
 // Measured, with db (fastest of repeated calls, 8-bit checkpoint of the same type; the range is that of several cards):
-//   bf16  rows 4096, 4096 x 4096:   123 to 131 us, 1050 to 1120 TFLOP/s      rows 8192, 11008 x 4096:  642 to 683 us, 1080 to 1150 TFLOP/s
+//   bf16  rows 4096, 4096 x 4096:   123 to 131 us, 1050 to 1120 TFLOP/s      rows 8192, 11008 x 4096:  642 to 703 us, 1050 to 1150 TFLOP/s
 //   fp32  rows 4096, 4096 x 4096:   335 to 355 us,  390 to 410 TFLOP/s (three times that of bf16 products)
 //   bf16  rows 32, 1024 x 1024:     10 us, a launch and its call      fp32  rows 1000, 1333 x 999:  29 us
 // Added to what is there, the first two take 187 and 933 us: every row of a wave's tile waits for its own read.
